@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_dense_general_kernel(const Ge
             }
         }
         // ---- the tile's rows, or this worker's part of them
+        __syncthreads();                                             // every warp has read the last block's factors
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
         const bool some = l_run > 0.f || l_run != l_run;               // NaN stays NaN
