@@ -25,11 +25,13 @@
 // pages to the swizzled tiles).  q and P keep their precision as sums of two e4m3
 // numbers, x = hi + lo: hi = e4m3(x), lo = e4m3(x - hi) hold 8 significant bits, all
 // of a bf16, so S = Q_hi K + Q_lo K is exact but for elements below 2^-10 of their
-// row's largest (absolute error 2^-17 of that), and P is off by at most 2^-9, as
-// a bf16 would be.  Two fp8 MMAs take as long as one 16-bit MMA.  The token scale
-// multiplies the fp32 scores; for O it is folded into P, and the running maximum is
-// taken over score + log2 of the block's largest scale (of each key's own where they
-// are far apart), so that P x scale stays inside e4m3 whatever the scales are.
+// row's largest (absolute error 2^-17 of that).  Two fp8 MMAs take as long as one 16-bit
+// MMA.  The token scale multiplies the fp32 scores; for O it is folded into P, and the
+// running maximum m is taken over score + log2 of the scale, so that P x scale stays inside
+// e4m3 whatever the scales are (within 2^+-60).  P x scale is off by at most 2^-9 of itself, as a
+// bf16 would be, plus what is below e4m3's last step, 2^-16 of the row's largest: that is
+// rounded up or down by an offset that varies with the key, so that it is right on average, and m
+// goes down again where a long context lies far below an early key.
 //
 // bf16 latents use kind::f16, Q and P in bf16, and tiles of 64 keys (the same bytes): a
 // block of 128 keys is two of them, one after the other, under one softmax (blocks of 64
@@ -73,8 +75,17 @@ constexpr int kOffP = kOffV + 2 * kVBytes;
 constexpr int kOffMeta = kOffP + kPBytes;
 constexpr uint32_t kSCol = 256;          // TMEM: O in columns 0-255, two score buffers of 64
 constexpr uint32_t kTmemCols = 512;
-constexpr float kGrow = 1.75f;           // FP8: the running maximum is refreshed past 2^1.75 (bf16: 2^8) ...
+constexpr float kGrow = 1.75f;           // FP8: the reference m follows the block's maximum up past 2^1.75 (bf16: 2^8) ...
 constexpr float kHead = 7.f;             // ... and P is held times 2^7: at most 2^8.75 < 448
+// ... and down to the recent blocks' maximum (which fades by kFade a block) where that is kGap or
+// more below and the rounding of P could be seen: u holds the sum of the squares of the blocks' largest
+// P over 2^7, less kNoise a block.  A key's rounding has a variance of 2^-20 at most, a block's 2^-13:
+// u < 0 is more than 2^-21 of sum P^2, an error of 2^-10.5 of the row's rms; where a maximum within
+// kGap comes back every kGap / kFade blocks it is 2^-10 at most.  (Chunk of 1024 tokens at 16384, 128
+// heads: 2.87 ms, 2.81 without falling, 2.94 with kNoise four times this.)
+constexpr float kGap = 2.f, kFade = 0.25f, kNoise = 0.015625f;
+constexpr float kDeep = 24.f;            // at most so far at a time: O and l stay inside fp32
+constexpr uint32_t kFarBits = 0x01400000u;   // neighbours' scales whose bits differ by more, 2^2.5 or so, are far apart
 
 // Barriers of a CTA.  Those that tell the MMA warp what is ready (K, V, P and Q
 // tiles, score buffers and O free) count both CTAs' arrivals in the even CTA.
@@ -90,11 +101,11 @@ struct PieceInfo {
 };
 struct Meta {
     float scale[2][128];
+    float lgp[2][64];            // log2 of the larger scale of two neighbours
     float mx[4][64];
-    int8_t qe[4][64];
+    int8_t qe[2][64];
     int unit[2][4];
-    float lg[2];
-    int edge[2];                 // bit 0: a mask is needed, bit 1: scales more than 2^3 apart
+    int edge[2];                 // bit 0: a mask is needed, bit 1: neighbours' scales far apart
     uint64_t bar[kBars];
     DenseCut cut[2];
     PieceInfo piece[2];
@@ -219,6 +230,12 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool x
                  : "r"(id), "r"(count), "r"(x ? 1u : 0u)
                  : "memory");
     return r != 0;
+}
+
+// log2 of a scale's magnitude, given as bits, from above by at most 0.09, within +-60.
+__device__ __forceinline__ float log2_above(uint32_t bits)
+{
+    return fminf(60.f, fmaxf(-60.f, fmaf(static_cast<float>(static_cast<int>(bits)), 0x1p-23f, -126.91f)));
 }
 
 // x -> hi + lo in e4m3, two values at a time.
@@ -661,7 +678,8 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     const uint64_t row = __shfl_sync(0xffffffffu, mine, e / kPer);
                     const int off = (e % kPer) * 32 + lane, x = __shfl_sync(0xffffffffu, pos, e / kPer) + off;
                     const bool some = x < t.last.hi && (x >= t.first.lo || x < t.last.sink);
-                    v[e] = some && row ? *reinterpret_cast<const float*>(row + (e % kPer) * 32 * p.c.sts + step) : 0.f;
+                    // (-0 marks a key that no row sees)
+                    v[e] = some && row ? *reinterpret_cast<const float*>(row + (e % kPer) * 32 * p.c.sts + step) : -0.f;
                 }
             };
             if (pc.blk0 < pc.blk1 && t.over && rank == 0 && lane == 0 && p.status)
@@ -684,34 +702,43 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(sc + (U - 1) * p.c.sts));
                 }
                 if (j > pc.blk0) {
-                    const int st = n & 1;
-                    ok = wait_bar(bar(kMEmpty + st), ((n >> 1) & 1) ^ 1, abort);
-                    if (!ok)
-                        return;
                     const bool bad = pos >= 0 && pl.page >= p.c.num_pages;
                     const bool whole = pos >= 0 && pos + U <= t.first.hi && (pos >= t.last.lo || pos + U <= t.first.sink);
                     const bool edge = __any_sync(0xffffffffu, lane < per_block && (bad || !whole));
                     if (bad && rank == 0 && p.status)
                         atomicOr(p.status, DSA_DEV_BAD_INDEX);
-                    if (lane < per_block)
-                        mt.unit[st][lane] = pos >= 0 && !bad ? pos : -1;
-                    uint32_t top = 0, low = 0xFFFFFFFFu;         // |scale| as bits, which order like values
+                    // even lanes take the pairs of keys 0-63, odd lanes those of 64-127
+                    const bool odd = lane & 1;
+                    bool far = false;
+                    float lg[2];
                     if (kFp8) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            mt.scale[st][e * 32 + lane] = w[e];
-                            const uint32_t a = __float_as_uint(fabsf(w[e]));
-                            top = max(top, a > 0x7F800000u ? 0u : a);            // NaN does not count
-                            low = min(low, a == 0 ? 0xFFFFFFFFu : a);
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t x = __float_as_uint(odd ? w[2 + e] : w[e]);
+                            const uint32_t o = __shfl_xor_sync(0xffffffffu, __float_as_uint(odd ? w[e] : w[2 + e]), 1);
+                            // magnitudes as bits, which differ by about 2^23 log2 of their ratio
+                            const uint32_t ax = x & 0x7FFFFFFFu, ao = o & 0x7FFFFFFFu, hi = max(ax, ao);
+                            far |= hi - min(ax, ao) > kFarBits && x != 0x80000000u && o != 0x80000000u;
+                            lg[e] = log2_above(hi);
                         }
-                        top = __reduce_max_sync(0xffffffffu, top);
-                        low = __reduce_min_sync(0xffffffffu, low);
+                        far = __any_sync(0xffffffffu, far);
                     }
-                    if (lane == 0) {
-                        const float hi = __uint_as_float(top);
-                        mt.lg[st] = kFp8 ? fminf(60.f, fmaxf(-60.f, log2f(hi))) : 0.f;      // log2(0) = -inf
-                        mt.edge[st] = (edge ? 1 : 0) | (kFp8 && hi > 8.f * __uint_as_float(low) ? 2 : 0);
+                    const int st = n & 1;
+                    ok = wait_bar(bar(kMEmpty + st), ((n >> 1) & 1) ^ 1, abort);
+                    if (!ok)
+                        return;
+                    if (lane < per_block)
+                        mt.unit[st][lane] = pos >= 0 && !bad ? pos : -1;
+                    if (kFp8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mt.scale[st][e * 32 + lane] = w[e];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            mt.lgp[st][((odd ? 2 : 0) + e) * 16 + (lane >> 1)] = lg[e];
                     }
+                    if (lane == 0)
+                        mt.edge[st] = (edge ? 1 : 0) | (far ? 2 : 0);
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(bar(kMFull + st));
@@ -782,7 +809,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         int e2 = max(-100, min(100, ((top & 0x7F) <= 96 ? 135 : 134) - (top >> 7)));
                         e2 = top == 0 ? 0 : top >= 0x7F80 ? 127 : e2;
                         if (lane == 0)
-                            mt.qe[which & 3][qr] = static_cast<int8_t>(e2);
+                            mt.qe[which & 1][qr] = static_cast<int8_t>(e2);
                         sc = e2 == 127 ? 1.f : __int_as_float((127 + e2) << 23);
                     }
 #pragma unroll
@@ -839,6 +866,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const DenseKeys keys = g >= 0 && m < pi.nrows ? dense_keys(s, pi.L, pi.n, (pi.m0 + m) / s.num_heads) : DenseKeys{0, 0, 0};
             float m_run = -INFINITY, l_run = 0.f, rf = 0.f;
             float n_run = 0.f;                                   // bf16: the sum of the rounded P
+            float rec = -INFINITY, u = 0.f;                      // FP8: what the reference goes down by
             for (int j = 0; j < nblk; ++j, ++n) {
                 const int b = n & 1;
                 const uint32_t ph = (n >> 1) & 1;
@@ -846,7 +874,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (ok)
                     ok = wait_bar(bar(kSFull + b), ph, abort);
                 if (ok && j == 0) {                              // (read before the score buffer is given back)
-                    const int e2 = kFp8 ? mt.qe[piece & 3][r] : 0;
+                    const int e2 = kFp8 ? mt.qe[piece & 1][r] : 0;
                     rf = e2 == 127 ? __int_as_float(0x7FC00000)
                                    : fmaxf(p.scale_log2 * __int_as_float((127 - e2) << 23), 1.17549435e-38f);
                 }
@@ -893,40 +921,71 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         x2[i] = pack_f32x2(x.x, x.y);
                     }
                 }
-                float m0 = -INFINITY, m1 = -INFINITY;
+                float mblk = -INFINITY;
+                if (kFp8 && !(kCold && (edge & 2))) {
+                    // score + log2 of the scale, of the larger scale of two neighbours (at most 2.6 too high)
+                    const ulonglong2* lg4 = reinterpret_cast<const ulonglong2*>(&mt.lgp[b][key0 / 2]);
+                    const uint64_t rf2 = pack_f32x2(rf, rf);
+                    float m1 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kC / 2; ++i) {
-                    const float2 x = unpack_f32x2(x2[i]);
-                    m0 = fmaxf(m0, x.x);
-                    m1 = fmaxf(m1, x.y);
-                }
-                m0 = fmaxf(m0, m1);
-                float mblk = m0 == -INFINITY ? -INFINITY : fmaf(m0, rf, mt.lg[b]);
-                if (kCold && kFp8 && (edge & 2)) {
-                    // scales far apart: a key's own log2, from above, in place of the block's:
-                    // log2(1 + f) <= f + 0.0861 for the mantissa f
-                    mblk = -INFINITY;
+                    for (int i = 0; i < kC / 8; ++i) {
+                        const ulonglong2 lg = lg4[i];
+                        const float2 a0 = unpack_f32x2(x2[4 * i]), a1 = unpack_f32x2(x2[4 * i + 1]);
+                        const float2 a2 = unpack_f32x2(x2[4 * i + 2]), a3 = unpack_f32x2(x2[4 * i + 3]);
+                        const float2 y0 = unpack_f32x2(fma_f32x2(pack_f32x2(fmaxf(a0.x, a0.y), fmaxf(a1.x, a1.y)), rf2, lg.x));
+                        const float2 y1 = unpack_f32x2(fma_f32x2(pack_f32x2(fmaxf(a2.x, a2.y), fmaxf(a3.x, a3.y)), rf2, lg.y));
+                        mblk = fmaxf(fmaxf(mblk, y0.x), y0.y);
+                        m1 = fmaxf(fmaxf(m1, y1.x), y1.y);
+                    }
+                    mblk = fmaxf(mblk, m1);
+                } else if (kFp8) {
+                    // neighbours' scales far apart: each key's own
 #pragma unroll
                     for (int i = 0; i < kC / 2; ++i) {
                         const float2 x = unpack_f32x2(x2[i]);
                         const float2 sc = *reinterpret_cast<const float2*>(&mt.scale[b][key0 + 2 * i]);
-                        const float a = fmaf(static_cast<float>(__float_as_int(sc.x) & 0x7FFFFFFF), 0x1p-23f, -126.91f);
-                        const float c = fmaf(static_cast<float>(__float_as_int(sc.y) & 0x7FFFFFFF), 0x1p-23f, -126.91f);
-                        mblk = fmaxf(mblk, fmaf(x.x, rf, fminf(60.f, fmaxf(-60.f, a))));
-                        mblk = fmaxf(mblk, fmaf(x.y, rf, fminf(60.f, fmaxf(-60.f, c))));
+                        mblk = fmaxf(mblk, fmaf(x.x, rf, log2_above(__float_as_uint(sc.x) & 0x7FFFFFFFu)));
+                        mblk = fmaxf(mblk, fmaf(x.y, rf, log2_above(__float_as_uint(sc.y) & 0x7FFFFFFFu)));
                     }
+                } else {
+                    float m1 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < kC / 2; ++i) {
+                        const float2 x = unpack_f32x2(x2[i]);
+                        mblk = fmaxf(mblk, x.x);
+                        m1 = fmaxf(m1, x.y);
+                    }
+                    mblk = fmaxf(mblk, m1) * rf;
                 }
                 named_bar_sync(bar_id, 128);                     // the block before has been read
                 *mx_mine = mblk;
                 named_bar_sync(bar_id, 128);
                 mblk = fmaxf(fmaxf(mt.mx[0][r], mt.mx[1][r]), fmaxf(mt.mx[2][r], mt.mx[3][r]));
-                if (mblk > m_run + (kFp8 ? kGrow : 8.f)) {
-                    f = m_run == -INFINITY ? 1.f : ex2_approx(m_run - mblk);
+                rec = fmaxf(mblk, rec - kFade);
+                const bool fall = kFp8 && u < 0.f && rec < m_run - kGap && mblk > -INFINITY;
+                if (mblk > m_run + (kFp8 ? kGrow : 8.f) || fall) {
+                    const float to = fall ? fmaxf(rec, m_run - kDeep) : mblk;
+                    f = m_run == -INFINITY ? 1.f : ex2_approx(m_run - to);
                     l_run *= f;
                     n_run *= f;
-                    m_run = mblk;
+                    u = fall ? f * f : u * f * f;                // (the sum held 1 at least before it fell)
+                    m_run = to;
                 }
                 const float m_use = m_run == -INFINITY ? 0.f : (kFp8 ? m_run - kHead : m_run);
+                // What P's last step, 2^-9, rounds: every other key gets the same offset of up to half
+                // a step either way, another one in each of the row's threads and in each block, so
+                // that P of 2^-10 and less do not all become 0 (131072 equal keys 12 nats below one: 13 %
+                // of the result were lost).  0 stays 0.
+                uint64_t dither = 0;
+                if constexpr (kFp8) {
+                    const float top = ex2_approx(mblk - (m_use + kHead));
+                    u = fmaf(top, top, u - kNoise);
+                    const uint32_t at = static_cast<uint32_t>(j) * 0x9E3779B9u + static_cast<uint32_t>(side * 2 + half) * 0x20000000u;
+                    auto offset = [&](uint32_t k) -> float {     // 2^-9 to 2^-8, less the middle
+                        return __uint_as_float((at + k) >> 9 | 0x3B000000u) - 0.0029296875f;
+                    };
+                    dither = pack_f32x2(offset(0), offset(0x80000000u));
+                }
                 {
                     const uint64_t rf2 = pack_f32x2(rf, rf), neg = pack_f32x2(-m_use, -m_use);
                     uint64_t l2 = pack_f32x2(0.f, 0.f), n2 = l2;
@@ -941,7 +1000,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                             const float2 y = unpack_f32x2(fma_f32x2(x2[2 * i + e], rf2, neg));
                             const uint64_t pp = pack_f32x2(ex2_approx(y.x), ex2_approx(y.y));     // -inf -> 0
                             l2 = add_f32x2(l2, pp);
-                            const float2 w = unpack_f32x2(kFp8 ? mul_f32x2(pp, e == 0 ? sv.x : sv.y) : pp);
+                            const float2 w = unpack_f32x2(kFp8 ? fma_f32x2(pp, e == 0 ? sv.x : sv.y, dither) : pp);
                             if constexpr (kFp8) {
                                 split_e4m3(__floats2half2_rn(w.x, w.y), &hi[e], &lo[e]);
                             } else {

@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+from dense_bounds import check_elements, check_rms, exact_rows
 from dense_cases import BF16, FP8, Call, Latents
 from deepseek_sparse_attention_mqa_gb300 import _abi, build
 
@@ -84,3 +85,88 @@ def _mag(c):
     seen = torch.arange(L, device=k.device)[None, :] <= (L - n + torch.arange(n, device=k.device))[:, None]
     p = torch.softmax(s.masked_fill(~seen[:, None, :], -math.inf), -1)
     return torch.einsum("nhk,kv->nhv", p, k[:, :c.d_v].abs())
+
+
+# ------------------------------------- probabilities far below the row's largest
+
+def _call(lat, L, news, heads, d_v=512, q=None, scale=1.0, seed=4):
+    c = Call(lat, [L], [news], heads, d_v, seed=seed, scale=scale)
+    if q is not None:
+        c.q.copy_(q.expand_as(c.q))
+    return c
+
+
+def _checked(c, elements=True, rows=None):
+    c.run()
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    rows = rows or [0, c.rows // 2, c.rows - 1]
+    ref, z, mag, noise, ds = exact_rows(c, rows)
+    check_rms(c.out[rows], ref)
+    if elements:
+        check_elements(c.out[rows], c.lse[rows], ref, z, mag, noise, ds)
+
+
+@pytest.mark.parametrize("L,news", [(16384, 160), (131072, 80)])
+@pytest.mark.parametrize("above,sd", [(10.0, 0.01), (12.0, 0.3), (12.5, 0.5), (13.0, 1.0), (14.0, 0.3)])
+@pytest.mark.parametrize("ratio", [1.0, 7.0])
+def test_one_heavy_key_above_a_flat_context(L, news, above, sd, ratio):
+    """A key (an attention sink) `above` nats over a long context whose values share a mean: each
+    of the others is 2^-14 to 2^-20 of it and together they weigh as much.  `ratio`: their token
+    scale over the heavy key's."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    lat = Latents(FP8, 576, 64, [L], seed=1)
+    k = 0.5 + torch.randn((L, 576), generator=g, device="cuda")
+    k[:, 575] = sd * torch.randn(L, generator=g, device="cuda")      # the score
+    k[:, 574] = 16.0 * ratio                                          # the token scale
+    k[9, 574], k[9, 575] = 16.0, above
+    _store(lat, 0, k)
+    q = 0.004 * torch.randn((1, 128, 576), generator=g, device="cuda")
+    q[..., 574], q[..., 575] = 0.0, 1.0
+    _checked(_call(lat, L, news, 128, q=q.to(torch.bfloat16)))
+
+
+@pytest.mark.parametrize("spread,shift,qscale", [(0.3, 0.0, 1.0), (0.3, 0.5, 1.0), (0.3, 0.5, 0.6), (0.0, 0.5, 1.7)])
+def test_scores_of_many_magnitudes(spread, shift, qscale):
+    """Random latents whose magnitudes vary: the largest of 70000 scores lies far above what most of
+    the softmax's mass does, in nats, and blocks' maxima differ by as much."""
+    lat = Latents(FP8, 576, 64, [70000], seed=2, spread=spread)
+    if shift:
+        _store(lat, 0, (lat.rows[0] + shift).float())
+    c = _call(lat, 70000, 80, 128, scale=1.0 / math.sqrt(192))
+    c.q.mul_(qscale)
+    _checked(c)
+
+
+@pytest.mark.parametrize("heads", [128, 16])
+def test_a_heavy_key_in_every_block(heads):
+    """One key of every 128 heavy by 10 nats, the first by 6 more."""
+    L = 32768
+    lat = Latents(FP8, 576, 64, [L], seed=1)
+    k = 0.5 + torch.randn((L, 576), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    k[:, 575] = 0.0
+    k[:, 574] = 20.0
+    k[::128, 575] = 10.0
+    k[0, 575] = 16.0
+    _store(lat, 0, k)
+    q = torch.zeros((1, heads, 576), device="cuda")
+    q[..., 575] = 1.0
+    _checked(_call(lat, L, 160, heads, q=q.to(torch.bfloat16)))
+
+
+def test_a_sink_and_then_rising_and_falling_contexts():
+    """The block maxima fall by 25 nats, come back by 20 and fall again."""
+    L = 65536
+    lat = Latents(FP8, 576, 64, [L], seed=1)
+    k = 0.5 + torch.randn((L, 576), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    lvl = torch.zeros(L, device="cuda")
+    lvl[16384:32768] = 20.0
+    lvl[32768:49152] = 8.0
+    k[:, 575] = lvl + 0.3 * torch.randn(L, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    k[:, 574] = 30.0
+    k[0, 575] = 25.0
+    _store(lat, 0, k)
+    q = torch.zeros((1, 128, 576), device="cuda")
+    q[..., 575] = 1.0
+    _checked(_call(lat, L, 80, 128, q=q.to(torch.bfloat16)))
