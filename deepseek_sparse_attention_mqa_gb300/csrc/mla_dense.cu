@@ -310,11 +310,35 @@ __global__ void __launch_bounds__(kThreads, 1) mla_dense_general_kernel(const Ge
                     sFac[srow] = f;
             }
             // a row that not every query row sees may hold infinities or NaN: as
-            // values they become zeros (0 x NaN is NaN); who sees it has its NaN in P
-            if (any_bad)
+            // values they become zeros (0 x NaN is NaN); who sees a NaN has it in P, and
+            // who sees an infinity, with P = 0 where its score is -inf, gets the NaN here
+            if (any_bad) {
+                for (int kk = 0; kk < kN; ++kk) {
+                    if (!sBad[kk])
+                        continue;
+#pragma unroll
+                    for (int a = 0; a < 8; ++a) {
+                        const int r = (a >> 1) * 16 + (a & 1) * 8 + (lane >> 2);
+                        if (r >= t.nrows || !(dense_mask32(dense_keys(s, t.L, t.n, (t.m0 + r) / s.num_heads), base) >> kk & 1u))
+                            continue;
+#pragma unroll
+                        for (int b = 0; b < kNT; ++b) {
+                            const int c = col0 + b * 8 + (lane & 3) * 2;
+                            if (c >= p.d_v)
+                                continue;
+                            const uint32_t v = *reinterpret_cast<const uint32_t*>(sK + (kk * pitch + c) * 2);
+                            if ((v & 0x7F80u) == 0x7F80u)
+                                o[a >> 1][b][2 * (a & 1)] = __int_as_float(0x7FC00000);
+                            if ((v & 0x7F800000u) == 0x7F800000u)
+                                o[a >> 1][b][2 * (a & 1) + 1] = __int_as_float(0x7FC00000);
+                        }
+                    }
+                }
+                __syncthreads();
                 for (int e = tid; e < kN * per_row; e += kThreads)
                     if (sBad[e / per_row])
                         *reinterpret_cast<uint4*>(sK + (e / per_row * pitch + e % per_row * 8) * 2) = make_uint4(0, 0, 0, 0);
+            }
             __syncthreads();
             // ---- O = O f + P V
 #pragma unroll

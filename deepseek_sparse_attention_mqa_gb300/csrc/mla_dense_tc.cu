@@ -97,7 +97,7 @@ enum Bar {
 
 // What the softmax needs of a piece; nblk < 0: no more.
 struct PieceInfo {
-    int nblk, row0, m0, nrows, L, n, slot, flags;
+    int nblk, row0, m0, nrows, L, n, slot, flags, seq;
 };
 struct Meta {
     float scale[2][128];
@@ -264,6 +264,38 @@ __device__ __noinline__ Place place_of(const DenseCache& c, int seq, int pos, in
             o.page = pg;
     }
     return o;
+}
+
+// The bf16 latents' values at dims [dim, dim + 32) that are infinite or NaN in a key that the row sees
+// and another row of its tile does not (the V warp makes such a value 0): bit per dim.  The keys
+// before the first token's end, from the last one's start on and in the first one's sinks
+// are seen by all.
+__device__ __noinline__ uint32_t masked_infinities(const TcParams& p, const PieceInfo& pi, const DenseKeys& row, int dim)
+{
+    const DenseKeys first = dense_keys(p.s, pi.L, pi.n, pi.m0 / p.s.num_heads);
+    const DenseKeys last = dense_keys(p.s, pi.L, pi.n, (pi.m0 + pi.nrows - 1) / p.s.num_heads);
+    uint32_t found = 0;
+    auto look = [&](int from, int to) {
+        for (int x = from; x < to; ++x) {
+            if ((x < row.lo && x >= row.sink) || (x < first.hi && (x >= last.lo || x < first.sink)))
+                continue;
+            const Place at = place_of(p.c, pi.seq, x, p.s.cap);
+            if (at.page >= p.c.num_pages)
+                continue;
+            const uint4* v = reinterpret_cast<const uint4*>(p.c.vals + at.page * p.c.vps + at.token * p.c.vts + dim * 2);
+            for (int i = 0; i < 4; ++i) {
+                const uint4 w4 = v[i];
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                for (int e = 0; e < 4; ++e)
+                    found |= ((w[e] & 0x7F80u) == 0x7F80u ? 1u : 0u) << (8 * i + 2 * e) |
+                             ((w[e] & 0x7F800000u) == 0x7F800000u ? 2u : 0u) << (8 * i + 2 * e);
+            }
+        }
+    };
+    look(max(first.hi, 0), row.hi);
+    look(row.lo, min(last.lo, min(first.hi, row.hi)));
+    look(first.sink, min(row.sink, min(first.hi, row.lo)));
+    return found;
 }
 
 // The blocks of a worker's pieces, one after another.
@@ -443,8 +475,9 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     if (pos + U <= t.first.hi && (pos >= t.last.lo || pos + U <= t.first.sink))
                         continue;                                // every row sees all of it
                     // rows that no query row sees become zeros, rows that some do not
-                    // see too if they hold infinities or NaN (0 x NaN is NaN; a row that
-                    // sees them has NaN scores anyway)
+                    // see too if they hold infinities or NaN (0 x NaN is NaN; who sees a NaN
+                    // has it in its score, who sees an infinity with a score of -inf gets its
+                    // NaN with the results)
                     wrote = true;
                     constexpr int kSeg = kVC * 8;                // 16-byte segments a row
                     for (int e = lane; e < U * kSeg; e += 32) {
@@ -638,6 +671,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     o.L = t.L;
                     o.n = t.n;
                     o.slot = pc.slot;
+                    o.seq = t.seq;
                     o.flags = 1 | (pc.blk0 == 0 ? 2 : 0) | (pc.blk1 == t.nblk ? 4 : 0);
                     // the piece's q rows to L2: they are read a few blocks later
                     const int rows = min(64, t.nrows - rank * 64);
@@ -867,6 +901,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             float m_run = -INFINITY, l_run = 0.f, rf = 0.f;
             float n_run = 0.f;                                   // bf16: the sum of the rounded P
             float rec = -INFINITY, u = 0.f;                      // FP8: what the reference goes down by
+            bool inf_seen = false;                               // bf16: a score of -inf where a mask is needed
             for (int j = 0; j < nblk; ++j, ++n) {
                 const int b = n & 1;
                 const uint32_t ph = (n >> 1) & 1;
@@ -916,6 +951,8 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                     for (int i = 0; i < kC / 2; ++i) {
                         float2 x = unpack_f32x2(x2[i]);
+                        if (!kFp8)
+                            inf_seen |= (x.x == -INFINITY && (see >> (2 * i) & 1u)) || (x.y == -INFINITY && (see >> (2 * i + 1) & 1u));
                         x.x = see >> (2 * i) & 1u ? x.x : -INFINITY;
                         x.y = see >> (2 * i + 1) & 1u ? x.y : -INFINITY;
                         x2[i] = pack_f32x2(x.x, x.y);
@@ -1094,9 +1131,11 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int slot = pi.slot;
             const int64_t row = static_cast<int64_t>(pi.row0) + m;
             named_bar_sync(bar_id, 128);
-            *mx_mine = l_run;
+            *mx_mine = inf_seen ? -l_run : l_run;                // (sums of probabilities: the sign is free)
             named_bar_sync(bar_id, 128);
-            const float l = (mt.mx[0][r] + mt.mx[1][r]) + (mt.mx[2][r] + mt.mx[3][r]);
+            const float l = (fabsf(mt.mx[0][r]) + fabsf(mt.mx[1][r])) + (fabsf(mt.mx[2][r]) + fabsf(mt.mx[3][r]));
+            if (!kFp8)
+                inf_seen = (signbit(mt.mx[0][r]) || signbit(mt.mx[1][r]) || signbit(mt.mx[2][r]) || signbit(mt.mx[3][r])) && row_ok;
             if (any && ok)
                 ok = wait_bar(bar(kPvDone), (n & 1) ^ 1, abort);
             const bool some = l > 0.f || l != l;                 // NaN stays NaN
@@ -1141,9 +1180,19 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                             arrive_even(even(kOFree));
                     }
                 }
+                // (a row without a sum has zeros here, or NaN where it saw infinities)
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    o[i] = live && some ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+                    o[i] = live ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+                if constexpr (!kFp8) {
+                    if (inf_seen) {
+                        const uint32_t nan = masked_infinities(p, pi, keys, dim0 + (whole ? c * 32 : (c >> 1) * 32)) >>
+                                             (whole ? 0 : (c & 1) * 16);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = nan >> i & 1u ? 0x7FC00000u : o[i];
+                    }
+                }
                 if (whole) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {

@@ -170,3 +170,54 @@ def test_a_sink_and_then_rising_and_falling_contexts():
     q = torch.zeros((1, 128, 576), device="cuda")
     q[..., 575] = 1.0
     _checked(_call(lat, L, 80, 128, q=q.to(torch.bfloat16)))
+
+
+# ------------------------------------------------------------- seen infinities
+
+def _definition(c, window=None, sinks=0):
+    """out and lse of every row from the definition in 64 bits, infinities included: a key
+    with probability 0 still multiplies its value."""
+    k = c.lat.rows[0]
+    outs, lses = [], []
+    L, n = c.lens[0], c.rows
+    for i in range(n):
+        vis = min(max(L - n + i + 1, 0), L)
+        pos = torch.arange(vis, device=k.device)
+        keep = (pos >= vis - window) | (pos < sinks) if window is not None else torch.ones_like(pos, dtype=torch.bool)
+        x = k[pos[keep]]
+        s = c.scale * (c.q[i].double()[:, None, :] * x[None]).sum(-1)
+        z = torch.logsumexp(s, -1)
+        p = torch.exp(s - z[:, None])
+        outs.append((p[:, :, None] * x[None, :, :c.d_v]).sum(1))
+        lses.append(z)
+    return torch.stack(outs), torch.stack(lses)
+
+
+@pytest.mark.parametrize("heads,d_qk,d_v,page", [(16, 576, 512, 64), (128, 512, 512, 32), (4, 80, 64, 64), (16, 576, 512, 16),
+                                                 (3, 576, 512, 64)])
+@pytest.mark.parametrize("window", [None, 40])
+@pytest.mark.parametrize("where", [250, 120, 299])
+def test_seen_infinities_give_what_the_definition_gives(heads, d_qk, d_v, page, window, where):
+    """A bf16 latent with an infinity: where its score is -inf its probability is 0, and 0 x inf is NaN
+    in that element, whatever else the row's tile sees; where it is +inf or NaN the whole row is."""
+    lat = Latents(BF16, d_qk, page, [300], seed=3)
+    c = Call(lat, [300], [100], heads, d_v, seed=4)
+    bad = {where: (5, float("inf")), where - 3: (11, -float("inf")), 7: (d_qk - 1, float("inf"))}
+    c.q[..., 5] = -c.q[..., 5].abs() - 0.5                  # x inf: -inf
+    c.q[..., 11] = c.q[..., 11].abs() + 0.5
+    c.q[..., d_qk - 1] = -c.q[..., d_qk - 1].abs() - 0.5
+    c.q[50, 0, 5] = 1.0                                     # one row sees +inf
+    for p, (d, v) in bad.items():
+        lat.rows[0][p, d] = v
+        row = lat.values[int(lat.table[0, p // page]), (p % page) * lat.tok:(p % page + 1) * lat.tok]
+        row[:2 * d_qk].view(torch.bfloat16)[d] = v
+    c.run(window, 2)
+    torch.cuda.synchronize()
+    ref, z = _definition(c, window, 2)
+    assert torch.equal(torch.isnan(c.out), torch.isnan(ref.to(torch.bfloat16)))
+    fin = torch.isfinite(z)
+    assert torch.equal(torch.isfinite(c.lse), fin)
+    ok = ~torch.isnan(ref)
+    # |out| < 8 here: 2^-8 of itself, and of the values' sum, as everywhere
+    assert bool(((c.out.double() - ref)[ok].abs() <= 2.0 ** -8 * ref[ok].abs() + 0.03).all())
+    assert bool(((c.lse.double() - z)[fin].abs() <= 1e-3).all())
