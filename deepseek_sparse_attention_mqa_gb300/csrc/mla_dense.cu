@@ -272,12 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_dense_general_kernel(const Ge
             __syncthreads();
             // ---- softmax: thread (row, quad) has keys quad * 8 .. + 7
             {
-                const uint32_t see = dense_mask32(keys, base) >> (squad * 8);
+                uint32_t see = dense_mask32(keys, base) >> (squad * 8);
                 float x[8], mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const int kk = squad * 8 + c;
                     const bool on = (see >> c & 1u) && sValid[kk];
+                    see &= on ? 0xFFFFFFFFu : ~(1u << c);
                     x[c] = on ? sS[srow * kSPitch + kk] * (p.scale_log2 * (kFp8 ? sScale[kk] : 1.f)) : -INFINITY;
                     mx = fmaxf(mx, x[c]);
                 }
@@ -296,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_dense_general_kernel(const Ge
                     for (int e = 0; e < 2; ++e) {
                         const float pr = ex2_approx(x[c + e] - m_use);          // a key not seen: 2^-inf = 0
                         sum += pr;
-                        pv[e] = x[c + e] == -INFINITY ? 0.f : pr * (kFp8 ? sScale[squad * 8 + c + e] : 1.f);
+                        // (0 times a seen token's infinite scale is NaN, an unseen token's scale is no matter)
+                        pv[e] = see >> (c + e) & 1u ? pr * (kFp8 ? sScale[squad * 8 + c + e] : 1.f) : 0.f;
                     }
                     const __nv_bfloat162 b = __floats2bfloat162_rn(pv[0], pv[1]);
                     const __nv_bfloat162 d = __floats2bfloat162_rn(pv[0] - __low2float(b), pv[1] - __high2float(b));

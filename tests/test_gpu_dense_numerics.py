@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from dense_bounds import check_elements, check_rms, exact_rows
-from dense_cases import BF16, FP8, Call, Latents
+from dense_cases import BF16, FP8, Call, Latents, check
 from deepseek_sparse_attention_mqa_gb300 import _abi, build
 
 pytestmark = pytest.mark.gpu
@@ -221,3 +221,22 @@ def test_seen_infinities_give_what_the_definition_gives(heads, d_qk, d_v, page, 
     # |out| < 8 here: 2^-8 of itself, and of the values' sum, as everywhere
     assert bool(((c.out.double() - ref)[ok].abs() <= 2.0 ** -8 * ref[ok].abs() + 0.03).all())
     assert bool(((c.lse.double() - z)[fin].abs() <= 1e-3).all())
+
+
+@pytest.mark.parametrize("heads,d_qk,d_v,page", [(16, 576, 512, 64), (4, 80, 64, 64), (128, 576, 512, 64)])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), -float("inf")])
+@pytest.mark.parametrize("window", [None, 40])
+def test_token_scales_that_are_not_finite(heads, d_qk, d_v, page, scale, window):
+    """An infinite or NaN token scale spoils the rows that see the token, whatever its score's sign, and
+    no others."""
+    lat = Latents(FP8, d_qk, page, [300], seed=3)
+    c = Call(lat, [300], [100], heads, d_v, seed=4)
+    bad = 250
+    lat.scales[int(lat.table[0, bad // page]), bad % page] = scale
+    c.run(window, 2)
+    torch.cuda.synchronize()
+    saw = torch.zeros(100, dtype=torch.bool, device="cuda")
+    saw[50:(50 + window) if window else None] = True
+    assert bool(torch.isnan(c.out[saw]).all())
+    ref = c.ref(window, 2)
+    check(c.out[~saw], c.lse[~saw], tuple(x[~saw] for x in ref))
