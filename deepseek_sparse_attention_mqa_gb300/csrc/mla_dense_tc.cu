@@ -838,13 +838,14 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                             m2 = __vmaxu2(m2, __vmaxu2(v[a][e].z & 0x7FFF7FFFu, v[a][e].w & 0x7FFF7FFFu));
                         }
                         const int top = static_cast<int>(__reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16)));
-                        // times 2^e the largest, (1 + m / 128) 2^(E - 127), lies in [224, 448]; 127 marks
-                        // a row with infinities or NaN
+                        // times 2^e the largest, (1 + m / 128) 2^(E - 127), lies in [224, 448]; a row
+                        // with infinities or NaN becomes NaN as a whole, and so its scores (but not
+                        // what stands for the scores of keys that it does not see)
                         int e2 = max(-100, min(100, ((top & 0x7F) <= 96 ? 135 : 134) - (top >> 7)));
-                        e2 = top == 0 ? 0 : top >= 0x7F80 ? 127 : e2;
+                        e2 = top == 0 || top >= 0x7F80 ? 0 : e2;
                         if (lane == 0)
                             mt.qe[which & 1][qr] = static_cast<int8_t>(e2);
-                        sc = e2 == 127 ? 1.f : __int_as_float((127 + e2) << 23);
+                        sc = top >= 0x7F80 ? __int_as_float(0x7FC00000) : __int_as_float((127 + e2) << 23);
                     }
 #pragma unroll
                     for (int e = 0; e < 3; ++e) {
@@ -910,8 +911,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     ok = wait_bar(bar(kSFull + b), ph, abort);
                 if (ok && j == 0) {                              // (read before the score buffer is given back)
                     const int e2 = kFp8 ? mt.qe[piece & 1][r] : 0;
-                    rf = e2 == 127 ? __int_as_float(0x7FC00000)
-                                   : fmaxf(p.scale_log2 * __int_as_float((127 - e2) << 23), 1.17549435e-38f);
+                    rf = fmaxf(p.scale_log2 * __int_as_float((127 - e2) << 23), 1.17549435e-38f);
                 }
                 if (ok) {
                     tc_fence_after_sync();

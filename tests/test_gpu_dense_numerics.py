@@ -240,3 +240,27 @@ def test_token_scales_that_are_not_finite(heads, d_qk, d_v, page, scale, window)
     assert bool(torch.isnan(c.out[saw]).all())
     ref = c.ref(window, 2)
     check(c.out[~saw], c.lse[~saw], tuple(x[~saw] for x in ref))
+
+
+# ------------------------------------------------------ NaN scales and queries
+
+SMALL = [(BF16, 4, 80, 64, 64), (FP8, 4, 80, 64, 64), (BF16, 16, 576, 512, 64), (FP8, 16, 576, 512, 64), (FP8, 128, 512, 512, 32)]
+
+
+@pytest.mark.parametrize("fmt,heads,d_qk,d_v,page", SMALL)
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_queries_that_are_not_finite_in_rows_without_keys(fmt, heads, d_qk, d_v, page, value):
+    """A row that sees nothing gives 0 and -inf whatever its q holds, beside rows that see keys; also
+    where its keys' pages do not exist."""
+    lat = Latents(fmt, d_qk, page, [3, 200], seed=3)
+    lat.bt[1, :] = -1
+    c = Call(lat, [3, 200], [5, 1], heads, d_v, seed=4)
+    c.q[:2] = value
+    c.q[5, :, 3] = value
+    ref = c.ref()
+    c.run()
+    torch.cuda.synchronize()
+    assert _abi.device_status(c.status) == _abi.DEV_BAD_INDEX
+    for r in (0, 1, 5):
+        assert bool((c.out[r] == 0).all()) and bool((c.lse[r] == float("-inf")).all())
+    check(c.out[2:5], c.lse[2:5], tuple(x[2:5] for x in ref))
