@@ -122,6 +122,7 @@ struct TcParams {
     int rope;                            // d_qk == 576
     float scale_log2;                    // |softmax_scale| * log2(e), at least the smallest normal number
     uint32_t flip;                       // sign bits to flip in two bf16 of q (negative softmax_scale)
+    uint32_t nan;                        // bits to set in two bf16 of q (softmax_scale is NaN: q becomes NaN)
     __nv_bfloat16* out;
     float* lse;
     DensePartials part;
@@ -852,7 +853,8 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         const int sg = e * 32 + lane;
                         if (sg >= segs)
                             continue;
-                        const uint32_t w[4] = {v[a][e].x ^ p.flip, v[a][e].y ^ p.flip, v[a][e].z ^ p.flip, v[a][e].w ^ p.flip};
+                        const uint32_t w[4] = {(v[a][e].x ^ p.flip) | p.nan, (v[a][e].y ^ p.flip) | p.nan,
+                                               (v[a][e].z ^ p.flip) | p.nan, (v[a][e].w ^ p.flip) | p.nan};
                         if constexpr (kFp8) {
                             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -1271,8 +1273,9 @@ dsa_status launch_mla_dense_tc(const DenseArgs& a, const DeviceInfo& dev, cudaSt
     const int unit = fp8 && c->page_kv % 64 == 0 && !narrow ? 64 : 32;
     const float scale = a.softmax_scale * 1.4426950408889634f;
     const float mag = scale < 0.f ? -scale : scale;
-    p.scale_log2 = mag < 1.17549435e-38f ? 1.17549435e-38f : mag;     // (NaN stays)
+    p.scale_log2 = mag >= 1.17549435e-38f ? mag : 1.17549435e-38f;
     p.flip = scale < 0.f ? 0x80008000u : 0u;
+    p.nan = scale != scale ? 0x7FFF7FFFu : 0u;
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
     p.status = a.status;

@@ -264,3 +264,14 @@ def test_queries_that_are_not_finite_in_rows_without_keys(fmt, heads, d_qk, d_v,
     for r in (0, 1, 5):
         assert bool((c.out[r] == 0).all()) and bool((c.lse[r] == float("-inf")).all())
     check(c.out[2:5], c.lse[2:5], tuple(x[2:5] for x in ref))
+
+
+@pytest.mark.parametrize("fmt,heads,d_qk,d_v,page", SMALL)
+def test_nan_softmax_scale(fmt, heads, d_qk, d_v, page):
+    """NaN for every row that sees a key, 0 and -inf for those that see none."""
+    lat = Latents(fmt, d_qk, page, [3], seed=3)
+    c = Call(lat, [3], [5], heads, d_v, seed=4, scale=float("nan"))
+    c.run()
+    torch.cuda.synchronize()
+    assert bool((c.out[:2] == 0).all()) and bool((c.lse[:2] == float("-inf")).all())
+    assert bool(torch.isnan(c.out[2:]).all()) and bool(torch.isnan(c.lse[2:]).all())
