@@ -120,7 +120,7 @@ struct TcParams {
     DenseCache c;
     const __nv_bfloat16* q;
     int rope;                            // d_qk == 576
-    float scale_log2;                    // |softmax_scale| * log2(e), at least the smallest normal number
+    float scale_log2;                    // |softmax_scale| * log2(e)
     uint32_t flip;                       // sign bits to flip in two bf16 of q (negative softmax_scale)
     uint32_t nan;                        // bits to set in two bf16 of q (softmax_scale is NaN: q becomes NaN)
     __nv_bfloat16* out;
@@ -842,7 +842,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         // times 2^e the largest, (1 + m / 128) 2^(E - 127), lies in [224, 448]; a row
                         // with infinities or NaN becomes NaN as a whole, and so its scores (but not
                         // what stands for the scores of keys that it does not see)
-                        int e2 = max(-100, min(100, ((top & 0x7F) <= 96 ? 135 : 134) - (top >> 7)));
+                        int e2 = min(100, ((top & 0x7F) <= 96 ? 135 : 134) - (top >> 7));   // -120 at least
                         e2 = top == 0 || top >= 0x7F80 ? 0 : e2;
                         if (lane == 0)
                             mt.qe[which & 1][qr] = static_cast<int8_t>(e2);
@@ -913,7 +913,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     ok = wait_bar(bar(kSFull + b), ph, abort);
                 if (ok && j == 0) {                              // (read before the score buffer is given back)
                     const int e2 = kFp8 ? mt.qe[piece & 1][r] : 0;
-                    rf = fmaxf(p.scale_log2 * __int_as_float((127 - e2) << 23), 1.17549435e-38f);
+                    rf = fmaxf(p.scale_log2 * __int_as_float((127 - e2) << 23), __int_as_float(1));   // (times -inf it stays -inf)
                 }
                 if (ok) {
                     tc_fence_after_sync();
@@ -1273,7 +1273,7 @@ dsa_status launch_mla_dense_tc(const DenseArgs& a, const DeviceInfo& dev, cudaSt
     const int unit = fp8 && c->page_kv % 64 == 0 && !narrow ? 64 : 32;
     const float scale = a.softmax_scale * 1.4426950408889634f;
     const float mag = scale < 0.f ? -scale : scale;
-    p.scale_log2 = mag >= 1.17549435e-38f ? mag : 1.17549435e-38f;
+    p.scale_log2 = scale != scale ? 0.f : mag;
     p.flip = scale < 0.f ? 0x80008000u : 0u;
     p.nan = scale != scale ? 0x7FFF7FFFu : 0u;
     p.out = static_cast<__nv_bfloat16*>(a.out);

@@ -275,3 +275,18 @@ def test_nan_softmax_scale(fmt, heads, d_qk, d_v, page):
     torch.cuda.synchronize()
     assert bool((c.out[:2] == 0).all()) and bool((c.lse[:2] == float("-inf")).all())
     assert bool(torch.isnan(c.out[2:]).all()) and bool(torch.isnan(c.lse[2:]).all())
+
+
+@pytest.mark.parametrize("fmt,heads,d_qk,d_v,page", SMALL)
+@pytest.mark.parametrize("power", [100, 107, 108, 109, 112, 124])
+def test_queries_near_the_largest_bf16(fmt, heads, d_qk, d_v, page, power):
+    """Rows of q around 2^power, with a softmax_scale that brings their scores back.  (At 2^124 only
+    where q is scaled before it is multiplied; elsewhere the fp32 sums leave their range.)"""
+    if power == 124 and (fmt, d_v) != (FP8, 512):
+        return
+    lat = Latents(fmt, d_qk, page, [200, 90], seed=3, spread=0.0)
+    c = Call(lat, [200, 90], [3, 1], heads, d_v, seed=4, scale=2.0 ** -power / 14)
+    c.q.copy_((c.q.float().clamp(-4, 4) * 2.0 ** power).to(torch.bfloat16))
+    c.run()
+    torch.cuda.synchronize()
+    check(c.out, c.lse, c.ref())
