@@ -1253,7 +1253,9 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 bool mla_dense_tc_supported(const DenseArgs& a)
 {
     const dsa_paged_cache* c = a.kv;
-    return a.d_v == 512 && (a.d_qk == 512 || a.d_qk == 576) && c->page_kv % 32 == 0;
+    constexpr int64_t most = int64_t(1) << 40;           // a tensor map's strides lie below
+    return a.d_v == 512 && (a.d_qk == 512 || a.d_qk == 576) && c->page_kv % 32 == 0 &&
+           c->val_token_stride < most && c->val_page_stride < most;
 }
 
 dsa_status launch_mla_dense_tc(const DenseArgs& a, const DeviceInfo& dev, cudaStream_t stream)

@@ -290,3 +290,21 @@ def test_queries_near_the_largest_bf16(fmt, heads, d_qk, d_v, page, power):
     c.run()
     torch.cuda.synchronize()
     check(c.out, c.lse, c.ref())
+
+
+# ---------------------------------------------- strides past what a tensor map holds
+
+@pytest.mark.parametrize("fmt", [FP8, BF16])
+def test_page_stride_past_two_to_the_40(fmt):
+    """A cache of one page may state any page stride."""
+    lat = Latents(fmt, 576, 64, [60], seed=3)
+    c = Call(lat, [60], [2], 16, 512, seed=4)
+    page = int(lat.table[0, 0])
+    v = lat.values[page].clone()
+    s = lat.scales[page].clone() if fmt == FP8 else None
+    bt = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    c.cache = _abi.make_cache(fmt, 576, 64, 1, v, 1 << 41, lat.tok, s, 256 if fmt == FP8 else 0, 4 if fmt == FP8 else 0, bt)
+    c.run()
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    check(c.out, c.lse, c.ref())
