@@ -231,7 +231,7 @@ dsa_status launch_kv_gather(const GatherArgs& a, const DeviceInfo& dev, cudaStre
         per = (per + 1) / 2;
     p.rows_per_cta = per;
     p.recip = static_cast<uint32_t>((0x100000000ull + chunks - 1) / chunks);
-    const dim3 grid(static_cast<unsigned>((a.out_rows + per - 1) / per));
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.out_rows) + per - 1) / per));
     if (c->fmt == DSA_KV_FP8_E4M3) {
         if (a.bf16)
             kv_gather_kernel<DSA_KV_FP8_E4M3, true><<<grid, kThreads, 0, stream>>>(p);
