@@ -306,8 +306,17 @@ def mla_attention_workspace_bytes(rows, num_heads, d_qk, d_v, batch) -> int:
     return int(lib().dsa_mla_attention_workspace_bytes(rows, num_heads, d_qk, d_v, batch))
 
 
-def _check_dense(q, out, lse, d_v, seq_lens, cum_q):
-    """rows, heads and d_qk of a dense attention call; raises where the tensors do not fit."""
+def _check_batch(cache, batch, status):
+    import torch
+    if status is not None and (status.dtype is not torch.int32 or status.numel() < 1):
+        raise TypeError("status must be one int32")
+    kept = getattr(cache, "_keep", None)                # (a cache filled in by hand has none)
+    if kept is not None and kept[2].shape[0] < batch:
+        raise ValueError("the cache's block table must have a row for every sequence")
+
+
+def _check_dense(q, cache, out, lse, d_v, seq_lens, cum_q, batch, status):
+    """rows, heads, d_qk and batch of a dense attention call; raises where the tensors do not fit."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
     if q.dtype is not bf16 or out.dtype is not bf16 or lse.dtype is not torch.float32:
@@ -320,7 +329,12 @@ def _check_dense(q, out, lse, d_v, seq_lens, cum_q):
     if not (q.is_contiguous() and out.is_contiguous() and lse.is_contiguous() and seq_lens.is_contiguous()
             and (cum_q is None or cum_q.is_contiguous())):
         raise ValueError("q, out, lse, seq_lens and cum_q must be contiguous")
-    return rows, heads, d_qk
+    if batch is None:
+        batch = seq_lens.numel()
+    if seq_lens.numel() < batch or (cum_q is not None and cum_q.numel() <= batch):
+        raise ValueError("seq_lens must hold batch lengths, cum_q batch + 1 rows")
+    _check_batch(cache, batch, status)
+    return rows, heads, d_qk, batch
 
 
 def _addr(t):
@@ -333,10 +347,10 @@ def mla_attention(q_bf16, softmax_scale, cache: PagedCache, seq_lens, out, lse, 
                   next_n=1, workspace=None, status=None, stream=None):
     """mla_attention_paged: every new token attends to all of its sequence up to
     itself.  ``batch`` defaults to the length of ``seq_lens``."""
-    rows, heads, d_qk = _check_dense(q_bf16, out, lse, d_v, seq_lens, cum_q)
+    rows, heads, d_qk, batch = _check_dense(q_bf16, cache, out, lse, d_v, seq_lens, cum_q, batch, status)
     st = lib().mla_attention_paged(
         q_bf16.data_ptr(), rows, heads, d_qk, d_v, float(softmax_scale), cache, seq_lens.data_ptr(), _addr(cum_q),
-        seq_lens.shape[0] if batch is None else batch, next_n, out.data_ptr(), lse.data_ptr(), _addr(workspace),
+        batch, next_n, out.data_ptr(), lse.data_ptr(), _addr(workspace),
         0 if workspace is None else workspace.nbytes, _addr(status), _stream(stream))
     if st:
         _check(st, "mla_attention_paged")
@@ -346,10 +360,10 @@ def mla_attention_window(q_bf16, softmax_scale, cache: PagedCache, seq_lens, win
                          cum_q=None, batch=None, next_n=1, workspace=None, status=None, stream=None):
     """mla_attention_paged_window: every new token attends to the last ``window``
     tokens up to itself and to its sequence's first ``num_sinks``."""
-    rows, heads, d_qk = _check_dense(q_bf16, out, lse, d_v, seq_lens, cum_q)
+    rows, heads, d_qk, batch = _check_dense(q_bf16, cache, out, lse, d_v, seq_lens, cum_q, batch, status)
     st = lib().mla_attention_paged_window(
         q_bf16.data_ptr(), rows, heads, d_qk, d_v, float(softmax_scale), cache, window, num_sinks, seq_lens.data_ptr(),
-        _addr(cum_q), seq_lens.shape[0] if batch is None else batch, next_n, out.data_ptr(), lse.data_ptr(),
+        _addr(cum_q), batch, next_n, out.data_ptr(), lse.data_ptr(),
         _addr(workspace), 0 if workspace is None else workspace.nbytes, _addr(status), _stream(stream))
     if st:
         _check(st, "mla_attention_paged_window")
@@ -372,8 +386,13 @@ def kv_gather_dequantize(cache: PagedCache, cum_rows, starts, out, batch=None, s
     pitch, step = out.stride()
     if width < cache.head_dim or (rows and width > 1 and step != 1):
         raise ValueError("out must be [rows, >= head_dim] with unit stride along a row")
+    if batch is None:
+        batch = cum_rows.numel() - 1
+    if cum_rows.numel() < max(batch, 0) + 1 or (starts is not None and starts.numel() < batch):
+        raise ValueError("cum_rows must hold batch + 1 rows, starts batch positions")
+    _check_batch(cache, batch, status)
     st = lib().dsa_kv_gather_dequantize(
-        cache, cum_rows.data_ptr(), _addr(starts), cum_rows.shape[0] - 1 if batch is None else batch, out.data_ptr(),
+        cache, cum_rows.data_ptr(), _addr(starts), batch, out.data_ptr(),
         DTYPE_BF16 if bf16 else DTYPE_F32, pitch if rows > 1 else max(width, pitch), rows, _addr(status),
         _stream(stream))
     if st:
