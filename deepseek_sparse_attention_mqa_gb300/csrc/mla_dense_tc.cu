@@ -28,7 +28,7 @@
 // row's largest (absolute error 2^-17 of that).  Two fp8 MMAs take as long as one 16-bit
 // MMA.  The token scale multiplies the fp32 scores; for O it is folded into P, and the
 // running maximum m is taken over score + log2 of the scale, so that P x scale stays inside
-// e4m3 whatever the scales are (within 2^+-60).  P x scale is off by at most 2^-9 of itself, as a
+// e4m3 whatever the scales are (those below 2^-72 leave it at its lower end).  P x scale is off by at most 2^-9 of itself, as a
 // bf16 would be, plus what is below e4m3's last step, 2^-16 of the row's largest: that is
 // rounded up or down by an offset that varies with the key, so that it is right on average, and m
 // goes down again where a long context lies far below an early key.
@@ -233,10 +233,13 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool x
     return r != 0;
 }
 
-// log2 of a scale's magnitude, given as bits, from above by at most 0.09, within +-60.
+// log2 of a scale's magnitude, given as bits, from above by at most 0.09; kLeastScale at least, because
+// the probabilities' sum is held without the scale, 2^-lg times larger: up to 2^(8.75 + 72 + 24)
+// a key, where the reference fell by kDeep, and 2^127 for four million such keys.
+constexpr float kLeastScale = -72.f;
 __device__ __forceinline__ float log2_above(uint32_t bits)
 {
-    return fminf(60.f, fmaxf(-60.f, fmaf(static_cast<float>(static_cast<int>(bits)), 0x1p-23f, -126.91f)));
+    return fmaxf(kLeastScale, fmaf(static_cast<float>(static_cast<int>(bits)), 0x1p-23f, -126.91f));
 }
 
 // x -> hi + lo in e4m3, two values at a time.

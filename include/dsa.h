@@ -435,10 +435,20 @@ DSA_API dsa_status sparse_mla_decode_swa(const void* q_bf16, int rows, int num_h
  *           aligned; its contents need no initialisation and do not outlive the
  *           call.  Calls that overlap on the GPU need separate workspaces.
  * Supported: 16 <= d_qk <= 1024, 16 <= d_v <= min(d_qk, 512), multiples of 16;
- *           any num_heads with rows * num_heads < 2^31.  FP8 scores are formed from
- *           q split into two e4m3 parts a row (each element to 2^-17 of its row's
- *           largest) where the tensor-core kernel runs: d_v 512, d_qk 512 or 576,
- *           pages that are multiples of 32 tokens.
+ *           any num_heads with rows * num_heads < 2^31; max_pages_per_seq * page_kv
+ *           < 2^30.
+ * Rounding: scores, their maxima and sums are fp32.  Where the tensor-core kernel
+ *           runs (d_v 512, d_qk 512 or 576, pages that are multiples of 32 tokens,
+ *           strides below 2^40): over FP8 caches q is split into two e4m3 parts a row
+ *           (each element to 2^-17 of its row's largest) and a probability times its
+ *           token's scale likewise (2^-9 of itself; what lies below 2^-16 of the
+ *           largest is rounded right on average, an rms of at most 2^-10 of the row's),
+ *           for token scales of magnitude 2^-72 to 2^100, or 0; over BF16 caches a
+ *           probability is a bf16 (2^-8 of itself) and the output is divided by the
+ *           rounded probabilities' sum.  Elsewhere a probability is two bf16 (2^-17).
+ * Infinities and NaN: a row that sees a score of +inf or NaN gets NaN; a value that is
+ *           infinite or NaN times a probability of 0 is NaN in that element.  A row all
+ *           of whose scores are -inf gets lse = -inf and otherwise out = 0.
  * Results do not depend on how the work was divided beyond rounding, and are the
  * same on every call with the same arguments on one GPU model.
  * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY (ws_bytes), CUDA.

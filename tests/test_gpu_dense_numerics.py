@@ -308,3 +308,19 @@ def test_page_stride_past_two_to_the_40(fmt):
     torch.cuda.synchronize()
     assert int(c.status.item()) == 0
     check(c.out, c.lse, c.ref())
+
+
+@pytest.mark.parametrize("heads,d_qk,d_v,page", [(16, 576, 512, 64), (128, 512, 512, 32), (4, 80, 64, 64)])
+@pytest.mark.parametrize("power", [-58, -40, 40, 59, 62, 70, 100])
+def test_token_scales_of_far_powers(heads, d_qk, d_v, page, power):
+    """All token scales times 2^power, the scores brought back by the softmax_scale."""
+    lat = Latents(FP8, d_qk, page, [300, 90], seed=3)
+    lat.scales.mul_(2.0 ** power)
+    for b in range(2):
+        lat.scale_rows[b] *= 2.0 ** power
+        lat.rows[b] *= 2.0 ** power
+    c = Call(lat, [300, 90], [3, 1], heads, d_v, seed=4, scale=2.0 ** -power / 14)
+    c.run()
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    check(c.out, c.lse, c.ref())
