@@ -7,6 +7,10 @@ exact result once to bf16.  A probability held like a bf16 is off by as much,
 relative to itself, as the output's own rounding; where few keys carry a row that
 is as much again, sqrt(2) in all, and less where many do.
 
+``check_units``: for every unit of 32 keys, the error's component along what the unit adds
+to the result (sum p (v - out) over its keys) is a quarter of that at most, where an error
+of the rms that check_rms allows makes it a tenth or less by chance; a unit left out gives -1, one taken twice +1.
+
 ``check_elements``: each output within its own half step of bf16 (2^-8 of itself) and the
 same of sum_j p_j |v_j| for its probabilities, with what fp32 scores add (``ds``: their
 absolute error, in the probability and in its normaliser; 2^-20 for exp2 and sums), and
@@ -32,6 +36,38 @@ def rms(x):
 def check_rms(out, ref):
     err, once = rms(out.double() - ref), rms(ref.to(torch.bfloat16).double() - ref)
     assert err <= 2 * once, "rms error %.3e, %.2f times one rounding's" % (err, err / once)
+
+
+def check_units(out, ref, p, v, unit=32):
+    """out, ref: [heads, d_v] of one row; p: [heads, keys]; v: [keys, d_v]."""
+    # in units of the output's own rounding, so that all heads count
+    w = 1.0 / (ref.abs() + ref.pow(2).mean(-1, keepdim=True).sqrt())
+    err = (out.double() - ref) * w
+    noise = 2 * rms((ref.to(torch.bfloat16).double() - ref) * w)
+    n = p.shape[1]
+    tested = 0
+    for j in range(0, n, unit):
+        q = p[:, j:j + unit]
+        d = (q @ v[j:j + unit] - q.sum(-1, keepdim=True) * ref) * w
+        size = float((d ** 2).sum())
+        if noise > 0.1 / 6 * math.sqrt(size):                # six sigma of chance past a tenth
+            continue
+        tested += 1
+        a = float((err * d).sum()) / size
+        assert abs(a) <= 0.25, "keys %d to %d: %.2f of what they add" % (j, min(j + unit, n) - 1, a)
+    return tested
+
+
+def seen_of(c, b, i, window=None, sinks=0):
+    """(p [heads, keys], v [keys, d_v], out) in 64 bits of new token i of sequence b over the keys it sees."""
+    L, n = c.lens[b], c.news[b]
+    vis = min(max(L - n + i + 1, 0), L)
+    pos = torch.arange(vis, device=c.q.device)
+    if window is not None:
+        pos = pos[(pos >= vis - window) | (pos < sinks)]
+    k = c.lat.rows[b][pos]
+    p = torch.softmax(c.scale * (c.q[sum(c.news[:b]) + i].double() @ k.T), -1)
+    return p, k[:, :c.d_v], p @ k[:, :c.d_v]
 
 
 def check_elements(out, lse, ref, z, mag, noise, ds):

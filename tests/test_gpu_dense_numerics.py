@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from dense_bounds import check_elements, check_rms, exact_rows
+from dense_bounds import check_elements, check_rms, check_units, exact_rows, seen_of
 from dense_cases import BF16, FP8, Call, Latents, check
 from deepseek_sparse_attention_mqa_gb300 import _abi, build
 
@@ -324,3 +324,25 @@ def test_token_scales_of_far_powers(heads, d_qk, d_v, page, power):
     torch.cuda.synchronize()
     assert int(c.status.item()) == 0
     check(c.out, c.lse, c.ref())
+
+
+# ------------------------------------------------------------ long and cut contexts
+
+@pytest.mark.parametrize("fmt,heads,d_qk,d_v,page", [(FP8, 128, 576, 512, 64), (FP8, 16, 512, 512, 32), (BF16, 32, 576, 512, 64),
+                                                     (BF16, 64, 80, 64, 64), (FP8, 16, 576, 512, 16)])
+@pytest.mark.parametrize("lens,news,window", [([20000], [1], None), ([9001, 40, 15000, 0, 777], [1, 2, 3, 0, 1], None),
+                                              ([15000, 7000], [1, 2], 6000)])
+def test_cut_contexts_lose_and_repeat_no_block(fmt, heads, d_qk, d_v, page, lens, news, window):
+    """Row by row against the bound that one missing or repeated block of keys exceeds."""
+    lat = Latents(fmt, d_qk, page, lens, seed=heads)
+    c = Call(lat, lens, news, heads, d_v, seed=heads + 1)
+    c.run(window, 100)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    row = 0
+    for b, n in enumerate(news):
+        for i in range(n):
+            p, v, ref = seen_of(c, b, i, window, 100)
+            check_rms(c.out[row], ref)
+            assert check_units(c.out[row], ref, p, v) > 0
+            row += 1
