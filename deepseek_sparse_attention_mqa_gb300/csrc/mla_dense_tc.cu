@@ -63,6 +63,11 @@ namespace {
 
 constexpr int kM = 128;                  // query rows of a pair
 constexpr int kThreads = 384;
+// Tokens a TMA box, the unit in which keys are read.  (Boxes of 64 take half the TMA issues but leave
+// more unseen keys in a window's blocks: window 128, 64 rows of 128 heads 20.5 against 22.5 us;
+// 512, 2749 tokens x 64 heads 304 against 313; a 1024-token chunk at 16384 x 128 heads 2.92 against
+// 2.96 ms; the same within 1 % past 6000 keys.)
+constexpr int kUnit = 32;
 constexpr int kTileCost = 3;             // Q's preparation and the epilogue, in blocks
 constexpr int kMinBlocks = 4;
 constexpr int kQBytes = 64 * 576 * 2;    // hi and lo parts, or bf16
@@ -331,13 +336,14 @@ struct BlockWalk {
     }
 };
 
-// U: tokens a TMA box (a unit), 64 or 32.
-template <bool kFp8, int U>
+template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_r, const TcParams p)
 {
     constexpr int kN = 128;                      // keys a block
+    constexpr int U = kUnit;
+    static_assert(U == 32, "a lane a token");
     constexpr int kSub = kFp8 ? 1 : 2;           // K and V tiles (sub-blocks) a block
     constexpr int kSN = kN / kSub;               // keys a sub-block
     constexpr int kKR = kSN / 2;                 // K rows of a CTA
@@ -706,18 +712,17 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             auto scales = [&](const Place& pl, int pos, float (&v)[4]) {
                 if (!kFp8)
                     return;
-                // lane u finds unit u's row of scales, every lane reads the keys 32 e + lane
+                // lane e finds unit e's row of scales, every lane reads the keys 32 e + lane
                 const uint64_t mine = pl.page < p.c.num_pages
                                           ? reinterpret_cast<uint64_t>(p.c.scs + pl.page * p.c.sps + pl.token * p.c.sts) : 0;
                 const int64_t step = lane * p.c.sts;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    constexpr int kPer = U / 32;                 // e's a unit
-                    const uint64_t row = __shfl_sync(0xffffffffu, mine, e / kPer);
-                    const int off = (e % kPer) * 32 + lane, x = __shfl_sync(0xffffffffu, pos, e / kPer) + off;
+                    const uint64_t row = __shfl_sync(0xffffffffu, mine, e);
+                    const int x = __shfl_sync(0xffffffffu, pos, e) + lane;
                     const bool some = x < t.last.hi && (x >= t.first.lo || x < t.last.sink);
                     // (-0 marks a key that no row sees)
-                    v[e] = some && row ? *reinterpret_cast<const float*>(row + (e % kPer) * 32 * p.c.sts + step) : -0.f;
+                    v[e] = some && row ? *reinterpret_cast<const float*>(row + step) : -0.f;
                 }
             };
             if (pc.blk0 < pc.blk1 && t.over && rank == 0 && lane == 0 && p.status)
@@ -1271,11 +1276,6 @@ dsa_status launch_mla_dense_tc(const DenseArgs& a, const DeviceInfo& dev, cudaSt
     p.c = dense_cache(c);
     p.q = static_cast<const __nv_bfloat16*>(a.q);
     p.rope = a.d_qk == 576;
-    // A box of 64 tokens takes fewer TMA issues, one of 32 leaves fewer unseen keys in a narrow
-    // window's blocks (window 512, 16 sinks, a chunk of 2749 tokens: 324 us in boxes of 32, 330
-    // of 64; window 128, 64 decode rows: 25.0 and 26.6); past some 1024 keys they are few either way.
-    const bool narrow = a.window >= 0 && static_cast<int64_t>(a.window) + a.sinks <= 1024;
-    const int unit = fp8 && c->page_kv % 64 == 0 && !narrow ? 64 : 32;
     const float scale = a.softmax_scale * 1.4426950408889634f;
     const float mag = scale < 0.f ? -scale : scale;
     p.scale_log2 = scale != scale ? 0.f : mag;
@@ -1295,9 +1295,9 @@ dsa_status launch_mla_dense_tc(const DenseArgs& a, const DeviceInfo& dev, cudaSt
                               static_cast<uint64_t>(c->num_pages)};
     const uint64_t strides[3] = {static_cast<uint64_t>(c->val_token_stride), 128,
                                  static_cast<uint64_t>(c->val_page_stride)};
-    const uint32_t box = static_cast<uint32_t>(unit);
+    const uint32_t box = kUnit;
     const uint32_t kbox[4] = {static_cast<uint32_t>(elems), box,
-                              static_cast<uint32_t>(unit == sub / 2 ? chunks : 1), 1};
+                              static_cast<uint32_t>(kUnit == sub / 2 ? chunks : 1), 1};
     const uint32_t vbox[4] = {static_cast<uint32_t>(elems), box, static_cast<uint32_t>(fp8 ? 2 : 4), 1};
     CUtensorMap tm_k, tm_v, tm_r;
     dsa_status st = encode_tiled(&tm_k, dt, 4, c->values, dims, strides, kbox, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -1316,8 +1316,7 @@ dsa_status launch_mla_dense_tc(const DenseArgs& a, const DeviceInfo& dev, cudaSt
         if (st != DSA_OK)
             return st;
     }
-    auto kern = !fp8 ? mla_dense_tc_kernel<false, 32>
-                     : unit == 64 ? mla_dense_tc_kernel<true, 64> : mla_dense_tc_kernel<true, 32>;
+    auto kern = fp8 ? mla_dense_tc_kernel<true> : mla_dense_tc_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess)
         return cuda_fail(e);
@@ -1335,7 +1334,7 @@ dsa_status launch_mla_dense_tc(const DenseArgs& a, const DeviceInfo& dev, cudaSt
     if (e != cudaSuccess)
         return cuda_fail(e);
     st = check_launch();
-    if (st != DSA_OK || !dense_may_cut(a, kM, 128, unit, kMinBlocks))
+    if (st != DSA_OK || !dense_may_cut(a, kM, 128, kUnit, kMinBlocks))
         return st;
     return launch_dense_join(p.part, pairs, a, dev, stream);
 }
