@@ -346,3 +346,54 @@ def test_cut_contexts_lose_and_repeat_no_block(fmt, heads, d_qk, d_v, page, lens
             check_rms(c.out[row], ref)
             assert check_units(c.out[row], ref, p, v) > 0
             row += 1
+
+
+@pytest.mark.parametrize("heads,d_qk,d_v,page", [(16, 576, 512, 64), (128, 512, 512, 32), (4, 80, 64, 64)])
+@pytest.mark.parametrize("kind", ["negative", "zero", "mixed"])
+def test_token_scales_of_either_sign_and_zero(heads, d_qk, d_v, page, kind):
+    """Scales below zero flip their token, zeros among others give a key with score 0 and no value."""
+    lat = Latents(FP8, d_qk, page, [900, 90], seed=3)
+    for b, L in enumerate((900, 90)):
+        f = torch.ones(L, dtype=torch.float64, device="cuda")
+        if kind != "zero":
+            f[::3] = -1.0
+        if kind != "negative":
+            f[1::5] = 0.0
+        for j in range(-(-L // page)):
+            n = min(page, L - j * page)
+            lat.scales[int(lat.table[b, j]), :n] *= f[j * page:j * page + n].float()
+        lat.scale_rows[b] *= f
+        lat.rows[b] *= f[:, None]
+    c = Call(lat, [900, 90], [5, 90], heads, d_v, seed=4)
+    c.run()
+    torch.cuda.synchronize()
+    check(c.out, c.lse, c.ref())
+    c.run(64, 3)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    check(c.out, c.lse, c.ref(64, 3))
+
+
+def test_falling_references_and_cut_pieces_in_a_graph():
+    """A captured call over a context with an early heavy key, replayed: the same bits as the first call."""
+    L = 40000
+    lat = Latents(FP8, 576, 64, [L], seed=1)
+    k = 0.5 + torch.randn((L, 576), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    k[:, 575] = 0.0
+    k[:, 574] = 16.0
+    k[3, 575] = 12.0
+    _store(lat, 0, k)
+    q = torch.zeros((1, 128, 576), device="cuda")
+    q[..., 575] = 1.0
+    c = _call(lat, L, 20, 128, q=q.to(torch.bfloat16))
+    _checked(c)
+    out, lse = c.out.clone(), c.lse.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run()
+    for _ in range(2):
+        c.out.fill_(7)
+        c.ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, c.out) and torch.equal(lse, c.lse)
