@@ -11,9 +11,9 @@
 // sequence, its place in the cache and its scale, then the rows' elements are moved in
 // chunks of 16 output bytes (8 bf16 or 4 fp32), eight chunks a thread at a time, all loads
 // before the first store.  A row's chunks belong to consecutive lanes, so a warp's loads and
-// its stores are contiguous whatever the formats (16-byte loads, and so stores 32 or 128 bytes
-// apart, took 322 instead of 281 us for 1.07 M rows of 576 e4m3 to bf16, and 111 instead
-// of 51 us for MXFP4 to fp32).
+// its stores are contiguous whatever the formats: 1.07 M rows of 576 e4m3 to bf16 take 281 us,
+// 0.81 M rows of 64 e2m1 to fp32 49 us (an earlier form with 16-byte loads, and so stores 32 or
+// 128 bytes apart, 322 and 111).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -222,8 +222,8 @@ dsa_status launch_kv_gather(const GatherArgs& a, const DeviceInfo& dev, cudaStre
     p.status = a.status;
     const int chunk = a.bf16 ? 8 : 4;
     // rows a CTA: about two rounds of kInFlight chunks a thread, so that finding the rows is
-    // spread over more of them (one round: 55 instead of 53 us for MXFP4, four: 294 instead of
-    // 287 for FP8); fewer where the call would not fill the GPU
+    // spread over more of them (one round: 52 instead of 50 us for MXFP4, four: 289 instead of
+    // 282 for FP8, in turn); fewer where the call would not fill the GPU
     const int chunks = c->head_dim / chunk;
     int per = 2 * kThreads * kInFlight / chunks;
     per = per < 1 ? 1 : per > kMaxRows ? kMaxRows : per;

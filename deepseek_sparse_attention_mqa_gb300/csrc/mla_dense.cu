@@ -16,9 +16,10 @@
 // size of the output's own, made results up to 1.5 times as far off as the output's
 // rounding alone), and O += P V with every warp owning d_v / 8 columns of all 64 rows, in
 // registers.  Bound by its load - multiply - softmax chain, four
-// barriers and 1.7 us a block of 80-element rows (two decode rows of 4 heads, 317 keys: 25 us;
-// 129 TFLOP/s on a 1024-token chunk of 576 / 512): it is the kernel that is right for every
-// shape, not the fast one.
+// barriers and 1.7 us a block of 80-element rows (two decode rows of 4 heads, 317 keys: 24 us).
+// With 576 / 512 latents in pages of 16: 1024 tokens x 128 heads at 16384 37.4 ms (121 TFLOP/s), 64
+// decode rows x 128 heads at 8192 2.04 ms (the tcgen05 kernel with pages of 32: 2.92 ms and 0.14).  It is
+// the kernel that is right for every shape, not the fast one.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -35,8 +36,9 @@ constexpr int kM = 64;                // query rows a tile
 constexpr int kN = 32;                // keys a block (and a unit)
 constexpr int kThreads = 256;
 constexpr int kTileCost = 2;
-// A cut costs a second launch and its loads, about ten blocks: contexts of up to 1024
-// keys stay whole.
+// A cut costs a second launch and its loads, about ten blocks; contexts of up to 1024 keys
+// stay whole (two decode rows of 4 heads: 1023 keys whole 63 us, 1100 keys cut 42 us, so that the
+// border is on the safe side).
 constexpr int kMinBlocks = 16;
 constexpr int kPPitch = kN + 8;       // bf16 elements a row of P
 constexpr int kSPitch = kN + 1;       // floats a row of S
@@ -730,7 +732,6 @@ DenseCache dense_cache(const dsa_paged_cache* c)
     d.bt_stride = c->bt_row_stride;
     d.page_kv = c->page_kv;
     d.num_pages = c->num_pages;
-    d.max_pages = c->max_pages_per_seq;
     return d;
 }
 
@@ -781,7 +782,8 @@ bool dense_may_cut(const DenseArgs& a, int tile_rows, int block_keys, int unit, 
 dsa_status launch_dense_join(const DensePartials& part, int workers, const DenseArgs& a, const DeviceInfo& dev,
                              cudaStream_t stream)
 {
-    // a CTA a row, as many as run at once (and no more than the call has rows)
+    // a CTA a group of rows (eight, or one of many parts), as many as run at once and no more than
+    // the call has rows
     const int64_t rows = static_cast<int64_t>(a.rows) * a.num_heads;
     const int64_t most = static_cast<int64_t>(dev.sm_count) * 4;
     const cudaError_t e = launch_pdl(mla_dense_join_kernel, dim3(static_cast<unsigned>(rows < most ? rows : most)),

@@ -50,7 +50,7 @@ struct DenseCache {
     int64_t sps, sts;
     const int32_t* bt;
     int64_t bt_stride;
-    int page_kv, num_pages, max_pages;
+    int page_kv, num_pages;
 };
 
 // Partial results of cut tiles: slot s holds slot_rows x (d_v + 1) floats (O / l,
@@ -188,7 +188,8 @@ __device__ __forceinline__ long long dense_scan(long long v, long long* tmp, lon
     return before + x - v;
 }
 
-// Walks tiles in order; `left` = tiles of the current sequence from `tile` on.
+// A place in the tiles' order: tile `tile` of the `tiles` of sequence `seq`, whose rows of the call,
+// new tokens and length stand beside it.
 struct DenseWalk {
     int seq, tile, tiles, begin, rows, n, L;
 };

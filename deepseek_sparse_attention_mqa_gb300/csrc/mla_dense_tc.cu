@@ -7,10 +7,11 @@
 //
 // Bound by the tensor cores: a pair of a query row and a key costs 2 (d_qk + 512)
 // flops against (d_qk + 4) bytes a key for 128 rows.
-// Measured: 1024 new tokens x 128 heads over 16384 keys, 576 / 512, FP8: 2.60 ms in bursts
-// (1.74 PFLOP/s, tensor pipe 74 % active), 2.82-2.92 ms back to back at the card's power limit;
-// 64 single tokens x 128 heads over 8K-131K keys: 0.85 and 0.93-0.97 ms.  What bounds a block of
-// 128 keys is the softmax's chain, about 2700 cycles on eight warps against 2176 of MMAs.
+// Measured: 1024 new tokens x 128 heads over 16384 keys, 576 / 512, FP8: 2.66 ms in bursts
+// (1.70 PFLOP/s, tensor pipe 72 % active), 2.85-2.93 ms back to back at the card's power limit;
+// 64 single tokens x 128 heads over 8K-131K keys: 0.88 and 0.93-0.99 ms.  What bounds a block of
+// 128 keys is the softmax's chain on eight warps: about 3000 cycles with all that stands between blocks,
+// against 2176 of MMAs.
 //
 // One cluster of two CTAs owns a tile of 128 query rows and walks its keys with
 // cta_group::2 MMAs of M = 128, 64 rows a CTA.  That shape leaves each CTA's results
@@ -28,8 +29,8 @@
 // row's largest (absolute error 2^-17 of that).  Two fp8 MMAs take as long as one 16-bit
 // MMA.  The token scale multiplies the fp32 scores; for O it is folded into P, and the
 // running maximum m is taken over score + log2 of the scale, so that P x scale stays inside
-// e4m3 whatever the scales are (those below 2^-72 leave it at its lower end).  P x scale is off by at most 2^-9 of itself, as a
-// bf16 would be, plus what is below e4m3's last step, 2^-16 of the row's largest: that is
+// e4m3 whatever the scales are (those below 2^-72 leave it at its lower end).  P x scale is off by at most 2^-9 of itself (a
+// bf16 by 2^-8), plus what is below e4m3's last step, 2^-16 of the row's largest: that is
 // rounded up or down by an offset that varies with the key, so that it is right on average, and m
 // goes down again where a long context lies far below an early key.
 //
@@ -86,8 +87,8 @@ constexpr float kHead = 7.f;             // ... and P is held times 2^7: at most
 // more below and the rounding of P could be seen: u holds the sum of the squares of the blocks' largest
 // P over 2^7, less kNoise a block.  A key's rounding has a variance of 2^-20 at most, a block's 2^-13:
 // u < 0 is more than 2^-21 of sum P^2, an error of 2^-10.5 of the row's rms; where a maximum within
-// kGap comes back every kGap / kFade blocks it is 2^-10 at most.  (Chunk of 1024 tokens at 16384, 128
-// heads: 2.87 ms, 2.81 without falling, 2.94 with kNoise four times this.)
+// kGap comes back every kGap / kFade blocks it is 2^-10 at most.  (A chunk of 1024 tokens at 16384, 128
+// heads, takes 2 % longer than without falling, and 2 % more with kNoise four times this.)
 constexpr float kGap = 2.f, kFade = 0.25f, kNoise = 0.015625f;
 constexpr float kDeep = 24.f;            // at most so far at a time: O and l stay inside fp32
 constexpr uint32_t kFarBits = 0x01400000u;   // neighbours' scales whose bits differ by more, 2^2.5 or so, are far apart
@@ -542,7 +543,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         // S(n + 2) is issued before O(n): it needs nothing of P(n), and the tensor cores
         // work on it while P(n) is on its way.
         // (S's MMAs are issued by a rolled loop over the 128-byte chunks: unrolled, its code
-        // pushed the softmax's out of the instruction cache, 2.95 instead of 2.87 ms for 1024
+        // pushes the softmax's out of the instruction cache, 2.97 instead of 2.88 ms for 1024
         // tokens x 128 heads at 16384.)
         BlockWalk<kN> sw(s, U, pair, mt.cut), ow(s, U, pair, mt.cut);
         int nq = 0, nv = 0, sp = 0, op = 0;
@@ -1021,7 +1022,7 @@ mla_dense_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 const float m_use = m_run == -INFINITY ? 0.f : (kFp8 ? m_run - kHead : m_run);
                 // What P's last step, 2^-9, rounds: every other key gets the same offset of up to half
                 // a step either way, another one in each of the row's threads and in each block, so
-                // that P of 2^-10 and less do not all become 0 (131072 equal keys 12 nats below one: 13 %
+                // that P of 2^-10 and less do not all become 0 (131072 such keys 12 nats below one: 13 %
                 // of the result were lost).  0 stays 0.
                 uint64_t dither = 0;
                 if constexpr (kFp8) {
